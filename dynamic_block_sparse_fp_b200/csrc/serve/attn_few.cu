@@ -626,7 +626,9 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
   const bool whole = un.units == 1;
   const size_t part0 = whole ? 0 : (first_part(sp, kv) + un.part) * sp.rows;
   ok = ok && !*abort_flag;
-  // one row's result at 4 columns: out and lse, or the unit's partial result
+  // one row's result at 4 columns: out and lse, or the unit's partial result (whose
+  // maximum is -infinity where the row sees none of the unit's keys: any number in
+  // its place would be taken for a score when the units are joined)
   auto store = [&](int r, int d, float big, float l, float4 x) {
     if (whole) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
     }
     if (!ok) l = 0.f, x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (sp.cluster == 1) {
-      store(r, d, base, l, x);
+      store(r, d, big, l, x);
     } else {
       *reinterpret_cast<float4 *>(&sm.all_o[r][d]) = x;
       if (d == 0) sm.all_ml[r] = make_float2(big, l);
@@ -707,8 +709,7 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
           x.z = fmaf(f, y[c].z, x.z), x.w = fmaf(f, y[c].w, x.w);
         }
       }
-      const float base = big == -INFINITY ? 0.f : big;
-      store(r, d, base, l, x);
+      store(r, d, big, l, x);
     }
     cluster_sync();  // nobody leaves while its shared memory is read
   }
