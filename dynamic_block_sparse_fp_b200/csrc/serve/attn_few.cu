@@ -271,7 +271,10 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
   auto key_of = [](int i) { return MIXED ? (i >> 1) + (i & 1) * 4 : i; };
   const float scale2 = 1.4426950408889634f / sqrtf(float(HD));  // scale * log2(e)
   uint32_t qf[NB][HD / 16][2];
-  float factor[NB][2];  // of the scores of the lane's rows 8 b + 2 j4 + e
+  // Factor of the scores of the lane's rows 8 b + 2 j4 + e.  8 bits: times 2^-14, so
+  // that a sum (at most 2^31) times it is finite for every query.  (The product of the
+  // row's power and the key's may not be: 0 x infinity for a sum of 0.)
+  float factor[NB][2];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int r = rg * 16 + 8 * b + i8;
@@ -299,8 +302,9 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
       // q 2^(14 - x) with 2^x the row's largest: bf16's 8 bits fit fp16's 11, and
-      // what falls below fp16's smallest is below 2^-38 of the largest
-      const int x = max(int(big >> 7) - 127, -100);
+      // what falls below fp16's smallest is below 2^-38 of the largest (of queries
+      // below 2^-95, for which 2^(x - 28) scale2 would leave the normal range: 2^-133)
+      const int x = max(int(big >> 7) - 127, -95);
       const float up = power(14 - x);
 #pragma unroll
       for (int k = 0; k < HD / 16; ++k) {
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        factor[b][e] = scale2 * power(__shfl_sync(0xffffffffu, x, 4 * (2 * j4 + e)) - 14);
+        factor[b][e] = scale2 * power(__shfl_sync(0xffffffffu, x, 4 * (2 * j4 + e)) - 28);
     }
   }
   // pages of this unit that do not exist (their keys are hidden)
@@ -438,8 +442,10 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            y[b][2 * n + e] = (s[b][0][2 * n + e] + s[b][1][2 * n + e]) * (factor[b][e] * kf);
+          for (int e = 0; e < 2; ++e) {
+            const float x = (s[b][0][2 * n + e] + s[b][1][2 * n + e]) * factor[b][e];
+            y[b][2 * n + e] = NARROW ? x * kf * 16384.f : x;
+          }
       }
       if (part) {
 #pragma unroll

@@ -45,3 +45,36 @@ def test_units_without_a_visible_key_leave_the_others_alone(cache_dtype, q_len):
     ls = np64(lse).reshape(hkv, hq // hkv, q_len)
     for h in range(hkv):
         check_group(o[h], ls[h], x[h], kd[h], vd[h], length - q_len, 0, 0, BF, hidden)
+
+
+# ------------------------------------------------------ ends of the range --
+
+@pytest.mark.parametrize("cache_dtype", [BF, F8])
+@pytest.mark.parametrize("hq,q_len", [(2, 1), (8, 5), (8, 40)])
+@pytest.mark.parametrize("q_exp,k_exp,meet", [(100, 100, False), (127, 119, False),
+                                              (-110, 112, True), (-122, 119, True),
+                                              (110, -112, True), (127, -126, True)])
+def test_queries_and_keys_near_the_ends_of_their_range(cache_dtype, hq, q_len, q_exp, k_exp, meet):
+    """Large queries and keys in different channels have logits of 0; large ones and
+    small ones in the same channels have ordinary logits."""
+    hkv, d, page, length = 2, 128, 64, 300
+    cache = make_cache(cache_dtype, 5, hkv, page, d, 1)
+    b, table, _ = make_batch([length], [q_len], page, 5, 1)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    k, v = (torch.randn(1, hkv, length, d, generator=g, device=DEV).to(BF) for _ in range(2))
+    q = torch.randn(q_len * hq, d, generator=g, device=DEV).clamp(-1.9, 1.9).to(BF)
+    k = k.clamp(-1.9, 1.9)
+    if not meet:
+        k[..., :64], q[:, 64:] = 0, 0
+    # (two steps: 2^127 has no double in fp32)
+    q, k = q.double() * 2.0 ** q_exp, k.double() * 2.0 ** k_exp
+    q, k = q.to(BF), k.to(BF)
+    assert q.isfinite().all() and k.isfinite().all()
+    every = serve.Batch(b.page_table, b.kv_lens, max_q_len=length)
+    serve.kv_write(cache, every, k, v)
+    out, lse = serve.paged_attn(q, cache, b)
+    kd, vd = (sequence(x, table, 0, length, page) for x in contents(cache))
+    o, x = (np64(y).reshape(hkv, hq // hkv, q_len, d) for y in (out, q))
+    ls = np64(lse).reshape(hkv, hq // hkv, q_len)
+    for h in range(hkv):
+        check_group(o[h], ls[h], x[h], kd[h], vd[h], length - q_len, 0, 0, BF)
