@@ -61,7 +61,8 @@ struct FewSmem {
   float2 ml[WARPS][16];
   uint64_t full[G::SLOTS], empty[G::SLOTS];
   FindUnit find;
-  int abort_flag, poison;
+  int abort_flag;
+  int poison;  // bit 0: V held an infinity or a NaN; bit 1: and pages are missing
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -146,10 +147,6 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 }
 __device__ __forceinline__ float power(int e) {  // 2^e, -126 <= e <= 127
   return __uint_as_float(uint32_t(e + 127) << 23);
-}
-// Bits of infinities' and NaNs' exponent fields carried into the signs' places.
-__device__ __forceinline__ uint32_t odd16(uint32_t x) {
-  return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
 // RG: row groups of 16 (0: one of 8)
@@ -603,7 +600,7 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], x);
-  if (__any_sync(0xffffffffu, bad) && lane == 0) sm.poison = 1;
+  if (__any_sync(0xffffffffu, bad) && lane == 0) sm.poison = missing ? 3 : 1;
   __syncthreads();  // the ring is no longer read
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -721,11 +718,14 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
   }
   if (!NARROW && poison) {
     __syncthreads();  // the rows are written
-    for (int r = r_first + threadIdx.x * r_step; r < rt.rows; r += THREADS * r_step)
-      add_odd_values(P, seq, un.s, kv, kt, unit_first, unit_count,
-                            row_position(seq, rt, r), HD,
-                            whole ? out + (row0 + r) * HD : nullptr,
-                            whole ? nullptr : sp.part_o + (part0 + r) * HD);
+    // (a lane a row: at most 64 rows, whole warps)
+    static_assert(THREADS >= 64, "a thread for each row");
+    const int r = r_first + threadIdx.x * r_step;
+    const bool row = r < rt.rows;
+    add_odd_values<HD>(P, seq, rt, un.s, kv, kt, unit_first, unit_count,
+                       row_position(seq, rt, r), (poison & 2) != 0,
+                       row && whole ? out + (row0 + r) * HD : nullptr,
+                       row && !whole ? sp.part_o + (part0 + r) * HD : nullptr);
   }
 }
 

@@ -380,10 +380,10 @@ __global__ void __launch_bounds__(THREADS, 2)
               *reinterpret_cast<const uint4 *>(stage + (x << (lg + 4)) + ((c ^ (x & 7)) << 4));
       }
       __syncwarp();
-      if (poison && good && row_exists)
-        add_odd_values(P, seq, un.s, kv, kt, first_tile, ntile, pos, HD,
-                              whole ? out + (row0 + r) * HD : nullptr,
-                              whole ? nullptr : sp.part_o + (prow0 + r) * HD);
+      if (poison && good)
+        add_odd_values<HD>(P, seq, rt, un.s, kv, kt, first_tile, ntile, pos, missing != 0,
+                           row_exists && whole ? out + (row0 + r) * HD : nullptr,
+                           row_exists && !whole ? sp.part_o + (prow0 + r) * HD : nullptr);
       if (row_exists) {
         if (!whole)
           sp.part_ml[prow0 + r] = make_float2(m, l);

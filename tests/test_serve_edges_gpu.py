@@ -78,3 +78,73 @@ def test_queries_and_keys_near_the_ends_of_their_range(cache_dtype, hq, q_len, q
     ls = np64(lse).reshape(hkv, hq // hkv, q_len)
     for h in range(hkv):
         check_group(o[h], ls[h], x[h], kd[h], vd[h], length - q_len, 0, 0, BF)
+
+
+# ------------------------------------------- infinities and NaNs in values --
+
+def fastest(call, runs=5):
+    best = math.inf
+    for _ in range(runs):
+        a, z = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        call()
+        z.record()
+        z.synchronize()
+        best = min(best, a.elapsed_time(z))
+    return best
+
+
+ODD_CASES = [([16001], [1], 0, 0), ([700, 16001, 40], [1, 9, 3], 0, 0), ([9000, 2500], [1, 16], 90, 5),
+             ([12001], [200], 0, 0), ([9000, 300], [333, 2], 700, 70)]
+
+
+@pytest.mark.parametrize("missing", [False, True])
+@pytest.mark.parametrize("case", range(len(ODD_CASES)))
+def test_odd_values_reach_those_who_see_them_and_cost_little(case, missing):
+    """Infinities and NaNs in values all over long sequences: each row has those of
+    the keys that it sees (and what they make together), and no call takes 20 times as
+    long for them.  One of the pages is missing, or none."""
+    hq, hkv, d, page = 8, 2, 128, 64
+    kv_lens, q_lens, window, sinks = ODD_CASES[case]
+    n_pages = sum(-(-x // page) for x in kv_lens)
+    cache = make_cache(BF, n_pages, hkv, page, d, case)
+    b, table, off = make_batch(kv_lens, q_lens, page, n_pages, case)
+    g = torch.Generator(device=DEV).manual_seed(case)
+    q = torch.randn(b.total_q * hq, d, generator=g, device=DEV).to(BF)
+    hidden = [np.zeros(x, bool) for x in kv_lens]
+    s = int(np.argmax(kv_lens))
+    if missing:
+        gone = (kv_lens[s] - 80) // page if window else kv_lens[s] // page // 3
+        b.page_table[s, gone] = -1
+        hidden[s][gone * page:(gone + 1) * page] = True
+    ws = serve.workspace(cache, b, hq)
+    call = lambda: serve.paged_attn(q, cache, b, window=window, sinks=sinks, ws=ws)  # noqa: E731
+    clean, clean_lse = call()
+    quiet = fastest(call)
+    # where they stand: (key from the sequence's end, column, value)
+    odd = [(0, 3, math.inf), (0, 9, math.inf), (1, 9, -math.inf), (63, 17, math.nan),
+           (64, 20, -math.inf), (100, 21, math.inf), (700, 40, math.inf), (2000, 41, math.nan),
+           (kv_lens[s] - 3, 50, -math.inf), (kv_lens[s] - 65, 51, math.inf)]
+    want = np64(clean).copy()
+    rows = want[off[s] * hq:off[s + 1] * hq].reshape(hkv, hq // hkv, q_lens[s], d)
+    for back, col, x in odd:
+        key = kv_lens[s] - 1 - back
+        if hidden[s][key]:
+            continue
+        cache.v[int(table[s, key // page]), 1, key % page, col] = x
+        for t in range(q_lens[s]):
+            i = kv_lens[s] - q_lens[s] + t
+            if key <= i and (window == 0 or i - key < window or key < sinks):
+                with np.errstate(invalid="ignore"):  # inf - inf
+                    rows[1, :, t, col] += x
+    out, lse = call()
+    assert np.array_equal(np64(out), want, equal_nan=True)
+    assert torch.equal(lse, clean_lse)
+    assert fastest(call) <= 20 * quiet + 0.1
+    cache.v[int(table[s, (kv_lens[s] - 1) // page])] = math.nan
+    out, _ = call()
+    # (a sequence's rows are [hq, n_s, d]: the last token's)
+    assert out[off[s] * hq:off[s + 1] * hq].view(hq, q_lens[s], d)[:, -1].isnan().all()
+    assert fastest(call) <= 20 * quiet + 0.1
+    if missing:
+        assert serve.fp_serve_last_device_status() == DEVICE_CHECK
