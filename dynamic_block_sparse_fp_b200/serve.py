@@ -260,6 +260,15 @@ def workspace(cache: KVCache, batch: Batch, n_q_heads: int) -> torch.Tensor | No
     return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
 
 
+def _buffer(ws, device) -> None:
+    """Refuses a workspace that is not a plain buffer on `device` (an expanded view
+    says more bytes than it has)."""
+    if not isinstance(ws, torch.Tensor) or ws.device != device:
+        raise ValueError(f"the workspace must be a tensor on {device}")
+    if not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+
+
 # -------------------------------------------------------------------- calls --
 
 def window_attn(q, k, v, window: int, sinks: int = 0, with_lse: bool = True, stream=None):
@@ -338,8 +347,8 @@ def paged_attn(q, cache: KVCache, batch: Batch, window: int = 0, sinks: int = 0,
     lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if with_lse else None
     if ws is None:
         ws = workspace(cache, batch, heads)
-    elif ws.device != device:
-        raise ValueError(f"the workspace is on {ws.device}, expected {device}")
+    else:
+        _buffer(ws, device)
     ops._check(lib().fp_paged_attn(cache.ref, batch.ref, heads, _DTYPES[q.dtype], window, sinks,
                                    q.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(ws),
                                    ops._nbytes(ws), _raw_stream(device)), "fp_paged_attn")

@@ -148,3 +148,21 @@ def test_odd_values_reach_those_who_see_them_and_cost_little(case, missing):
     assert fastest(call) <= 20 * quiet + 0.1
     if missing:
         assert serve.fp_serve_last_device_status() == DEVICE_CHECK
+
+
+# ---------------------------------------------------------------- refusals --
+
+def test_workspaces_that_are_no_buffers_are_refused():
+    """(before anything is launched)"""
+    cache = make_cache(BF, 100, 2, 64, 128, 0)
+    b, _, _ = make_batch([6000], [1], 64, 100, 0, slack_pages=200)
+    q = torch.zeros(8, 128, dtype=BF, device=DEV)
+    n = serve.workspace(cache, b, 8).numel()
+    assert n > 0
+    for ws in (torch.empty(1, dtype=torch.uint8, device=DEV).expand(n),
+               torch.empty(2 * n, dtype=torch.uint8, device=DEV)[::2],
+               torch.empty(n, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace"):
+            serve.paged_attn(q, cache, b, ws=ws)
+    with pytest.raises(ops.FPError, match="FP_ERR_WORKSPACE"):
+        serve.paged_attn(q, cache, b, ws=torch.empty(n - 1, dtype=torch.uint8, device=DEV))
