@@ -223,7 +223,8 @@ FP_API fp_status fp_paged_attn(const fp_kv_cache *cache, const fp_batch *batch, 
   if (P.total_q == 0) return FP_OK;
   if (!q || !out) return FP_ERR_NULL;
   if (!al(q, 16) || !al(out, 16) || !al(lse, 4)) return FP_ERR_ALIGN;
-  const size_t need = fp_paged_attn_workspace(cache, batch, n_q_heads);
+  const size_t need =
+      dtype == FP_F32 ? 0 : fp_paged_attn_workspace(cache, batch, n_q_heads);
   if (need > 0 && (!ws || !al(ws, 256) || ws_bytes < need)) return FP_ERR_WORKSPACE;
   if ((s = check_device()) != FP_OK) return s;
   set_window(&P, window, sinks);

@@ -255,7 +255,8 @@ def _packed(x, name, cache, batch, heads, dtypes) -> int:
 
 
 def workspace(cache: KVCache, batch: Batch, n_q_heads: int) -> torch.Tensor | None:
-    """A device byte buffer of fp_paged_attn_workspace bytes, or None if 0."""
+    """A device byte buffer of fp_paged_attn_workspace bytes, or None if 0 (fp32
+    queries need none)."""
     n = lib().fp_paged_attn_workspace(cache.ref, batch.ref, n_q_heads)
     return torch.empty(n, dtype=torch.uint8, device=cache.device) if n else None
 
@@ -345,10 +346,10 @@ def paged_attn(q, cache: KVCache, batch: Batch, window: int = 0, sinks: int = 0,
             return paged_attn(q, cache, batch, window, sinks, with_lse, ws)
     out = torch.empty_like(q)
     lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if with_lse else None
-    if ws is None:
-        ws = workspace(cache, batch, heads)
-    else:
+    if ws is not None:
         _buffer(ws, device)
+    elif q.dtype != torch.float32:
+        ws = workspace(cache, batch, heads)
     ops._check(lib().fp_paged_attn(cache.ref, batch.ref, heads, _DTYPES[q.dtype], window, sinks,
                                    q.data_ptr(), out.data_ptr(), _ptr(lse), _ptr(ws),
                                    ops._nbytes(ws), _raw_stream(device)), "fp_paged_attn")

@@ -133,9 +133,9 @@ fp_status fp_kv_read(const fp_kv_cache *cache, const fp_batch *batch, fp_dtype d
  * caches, FP_F32 queries FP_F32 and FP_E4M3.  out is packed like q.
  * Workspace: fp_paged_attn_workspace bytes (0 for an invalid description, and
  * where none is needed), 256-byte aligned, not shared by calls that may run at
- * the same time.  Over an FP_E4M3 cache, chunks (max_q_len * Hq / Hkv > 64) take
- * room there for a bf16 copy of the cache, of which the pages that are read are
- * filled in.
+ * the same time; FP_F32 queries need none.  Over an FP_E4M3 cache, chunks
+ * (max_q_len * Hq / Hkv > 64) take room there for a bf16 copy of the cache, of
+ * which the pages that are read are filled in.
  */
 size_t fp_paged_attn_workspace(const fp_kv_cache *cache, const fp_batch *batch, int n_q_heads);
 fp_status fp_paged_attn(const fp_kv_cache *cache, const fp_batch *batch, int n_q_heads,

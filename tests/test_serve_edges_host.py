@@ -1,8 +1,11 @@
 """Host-side checks of the serving library's corners (no GPU needed)."""
 import pytest
 import torch
+from test_serve_host import FAKE, PAST, WS, L, batch, cache, needs_no_gpu, paged  # noqa: F401
 
-from dynamic_block_sparse_fp_b200 import serve
+from dynamic_block_sparse_fp_b200 import ops, serve
+
+NARROW = dict(dtype=serve.FP_E4M3, k_exps=FAKE, v_exps=FAKE)
 
 
 def test_a_workspace_is_a_plain_buffer():
@@ -13,3 +16,10 @@ def test_a_workspace_is_a_plain_buffer():
             serve._buffer(ws, here)
     with pytest.raises(ValueError, match="workspace"):
         serve._buffer(torch.empty(1000, device="meta"), here)
+
+
+@needs_no_gpu
+def test_fp32_queries_need_no_workspace(L):  # noqa: F811
+    b = batch(max_q_len=100, total_q=200)
+    assert paged(cache(**NARROW), b) == WS
+    assert paged(cache(**NARROW), b, dtype=ops.FP_F32) in PAST
