@@ -650,7 +650,8 @@ cudaError_t run(const Problem &P, const Split &sp, const void *q, void *out, flo
   if (e != cudaSuccess) return e;
   CUtensorMap mq, mk, mv;
   const uint64_t kv_rows = P.page == 0 ? uint64_t(P.n_seqs) * P.hkv * P.max_q_len
-                                       : uint64_t(P.n_pages) * P.hkv * P.page;
+                           : P.by_place ? uint64_t(P.n_seqs) * P.max_pages * P.hkv * P.page
+                                        : uint64_t(P.n_pages) * P.hkv * P.page;
   const uint32_t box = P.page == 0 || P.page > BN ? BN : P.page;
   const CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
   if (!encode_map(&mq, q, uint64_t(P.total_q) * P.hq, HD, 64, BM, false, swizzle) ||
@@ -680,11 +681,16 @@ Split tc_split(const Problem &P) {
   return sp;
 }
 
-// Workspace: the units' partial results, and bf16 copies of an 8-bit cache's pages
-// at the pages' own places.
+// The copies of an 8-bit cache's pages: by their place in the table, or by their
+// number where the cache has fewer pages than the table has places.
+long long copied_pages(const Problem &P) {
+  return std::min<long long>(P.n_pages, static_cast<long long>(P.n_seqs) * P.max_pages);
+}
+
+// Workspace: the units' partial results, and the copies.
 size_t carve_serve(const Problem &P, bool narrow, Split *sp, void **k, void **v, void *ws) {
   Carver c{static_cast<char *>(ws), sp->on ? carve(P, sp, ws) : 0};
-  const size_t cache = narrow ? size_t(P.n_pages) * P.hkv * P.page * P.d : 0;
+  const size_t cache = narrow ? size_t(copied_pages(P)) * P.hkv * P.page * P.d : 0;
   *k = c.take<__nv_bfloat16>(cache);
   *v = c.take<__nv_bfloat16>(cache);
   return c.off;
@@ -705,7 +711,8 @@ cudaError_t launch_attn_serve(const Problem &P, bool narrow, const void *q, void
   void *k, *v;
   carve_serve(P, narrow, &sp, &k, &v, ws);
   if (narrow) {
-    const cudaError_t e = launch_kv_widen(P, k, v, st);
+    W.by_place = copied_pages(P) < P.n_pages;
+    const cudaError_t e = launch_kv_widen(P, W.by_place, k, v, st);
     if (e != cudaSuccess) return e;
     W.k = k;
     W.v = v;

@@ -256,12 +256,14 @@ __global__ void __launch_bounds__(THREADS)
   }
 }
 
-// The keys of a sequence that its new tokens see, as bf16 where an 8-bit cache
-// holds them (16 codes a lane).  A page that two sequences share is written twice
-// with the same numbers; a page that does not exist is not written.
+// The keys of a sequence that its new tokens see, as bf16 (16 codes a lane), at
+// their place in the table or by their page's number.  By number, a page that two
+// sequences share is written twice with the same numbers; a page that does not exist
+// is not written.
 template <int D>
 __global__ void __launch_bounds__(THREADS)
-    kv_widen_kernel(const Problem P, uint4 *__restrict__ k, uint4 *__restrict__ v) {
+    kv_widen_kernel(const Problem P, bool by_place, uint4 *__restrict__ k,
+                    uint4 *__restrict__ v) {
   constexpr int LANES = D / 16, PER = THREADS / LANES;
   const int s = blockIdx.y, lane = threadIdx.x % LANES;
   const Seq q = load_seq(P, s);
@@ -277,16 +279,19 @@ __global__ void __launch_bounds__(THREADS)
     const int key = i < sinks ? i : first + i - sinks;
     const long long page = page_row(P, s, key >> P.shift, 0);
     if (page < 0) continue;
+    const long long place = static_cast<long long>(s) * P.max_pages + (key >> P.shift);
+    const long long first_row = by_place ? place * P.hkv * P.page : page;
     for (int h = 0; h < P.hkv; ++h) {
-      const long long row = page + h * P.page + (key & (P.page - 1));
+      const int in = h * P.page + (key & (P.page - 1));
+      const long long row = page + in, to = first_row + in;
       const uint4 c = src[row * LANES + lane];
       const uint32_t byte = exps[row];
       const Raw<__nv_bfloat16> a = raw(e4m3_values(c.x, byte), e4m3_values(c.y, byte),
                                        __nv_bfloat16()),
                                b = raw(e4m3_values(c.z, byte), e4m3_values(c.w, byte),
                                        __nv_bfloat16());
-      dst[(row * LANES + lane) * 2] = a.w[0];
-      dst[(row * LANES + lane) * 2 + 1] = b.w[0];
+      dst[(to * LANES + lane) * 2] = a.w[0];
+      dst[(to * LANES + lane) * 2 + 1] = b.w[0];
     }
   }
 }
@@ -354,7 +359,7 @@ cudaError_t launch_kv_read(const Problem &P, int cache_dtype, int dtype, void *k
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv_widen(const Problem &P, void *k, void *v, cudaStream_t st) {
+cudaError_t launch_kv_widen(const Problem &P, bool by_place, void *k, void *v, cudaStream_t st) {
   const long long keys = static_cast<long long>(P.max_pages) * P.page;
   const int per = THREADS / (P.d / 16);
   long long x = (keys + per - 1) / per;
@@ -362,9 +367,9 @@ cudaError_t launch_kv_widen(const Problem &P, void *k, void *v, cudaStream_t st)
   const dim3 grid(unsigned(x > most ? most : x), unsigned(P.n_seqs), 2);
   uint4 *kt = static_cast<uint4 *>(k), *vt = static_cast<uint4 *>(v);
   if (P.d == 64)
-    kv_widen_kernel<64><<<grid, THREADS, 0, st>>>(P, kt, vt);
+    kv_widen_kernel<64><<<grid, THREADS, 0, st>>>(P, by_place, kt, vt);
   else
-    kv_widen_kernel<128><<<grid, THREADS, 0, st>>>(P, kt, vt);
+    kv_widen_kernel<128><<<grid, THREADS, 0, st>>>(P, by_place, kt, vt);
   return cudaGetLastError();
 }
 

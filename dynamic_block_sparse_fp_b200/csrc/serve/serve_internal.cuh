@@ -18,6 +18,9 @@ using namespace fpi;
 struct Problem {
   int n_seqs, hq, hkv, g, d;
   int n_pages, page, shift, max_pages, max_q_len, total_q;  // page == 1 << shift
+  // The pages' vectors lie at [sequence, index in its row of the table], not at the
+  // pages' numbers (copies of what a batch reads).
+  int by_place;
   int window;  // > 0 (no window: a number above every length)
   int sinks;
   const int32_t *table, *kv_lens, *q_offsets;
@@ -56,12 +59,13 @@ __device__ __forceinline__ Seq load_seq(const Problem &P, int s) {
   return x;
 }
 
-// Row of (page, kv head, slot 0) in the cache's [n_pages * hkv * page, d], or -1
-// for a page that does not exist.
+// Row of (page, kv head, slot 0) of the keys and values, [pages * hkv * page, d], or
+// -1 for a page that does not exist.
 __device__ __forceinline__ long long page_row(const Problem &P, int s, int index, int kv) {
-  const int id = P.table[size_t(s) * P.max_pages + index];
+  const long long place = static_cast<long long>(s) * P.max_pages + index;
+  const int id = P.table[place];
   if (id < 0 || id >= P.n_pages) return -1;
-  return (static_cast<long long>(id) * P.hkv + kv) * P.page;
+  return ((P.by_place ? place : id) * P.hkv + kv) * P.page;
 }
 
 // The 4 codes of a word times 2^(byte - 127), exact (NaN for byte 255).
@@ -81,8 +85,8 @@ cudaError_t launch_kv_write(const Problem &P, int cache_dtype, int dtype, const 
                             const void *v, cudaStream_t st);
 cudaError_t launch_kv_read(const Problem &P, int cache_dtype, int dtype, void *k, void *v,
                            cudaStream_t st);
-// bf16 copies, at the pages' own places, of the 8-bit vectors that a batch reads.
-cudaError_t launch_kv_widen(const Problem &P, void *k, void *v, cudaStream_t st);
+// bf16 copies of the 8-bit vectors that a batch reads, by place or by page number.
+cudaError_t launch_kv_widen(const Problem &P, bool by_place, void *k, void *v, cudaStream_t st);
 // fp32 queries: CUDA-core attention over fp32 or (narrow) 8-bit vectors.
 cudaError_t launch_attn_rows(const Problem &P, bool narrow, const float *q, float *out,
                              float *lse, cudaStream_t st);

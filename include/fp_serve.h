@@ -134,8 +134,10 @@ fp_status fp_kv_read(const fp_kv_cache *cache, const fp_batch *batch, fp_dtype d
  * Workspace: fp_paged_attn_workspace bytes (0 for an invalid description, and
  * where none is needed), 256-byte aligned, not shared by calls that may run at
  * the same time; FP_F32 queries need none.  Over an FP_E4M3 cache, chunks
- * (max_q_len * Hq / Hkv > 64) take room there for a bf16 copy of the cache, of
- * which the pages that are read are filled in.
+ * (max_q_len * Hq / Hkv > 64) take room there for bf16 copies of
+ * min(n_pages, n_seqs * max_pages) pages, of which those that are read are filled
+ * in: 4 * Hkv * page_size * d bytes each.  (So over a cache that fills the device,
+ * chunks are called with a table of their own sequences only.)
  */
 size_t fp_paged_attn_workspace(const fp_kv_cache *cache, const fp_batch *batch, int n_q_heads);
 fp_status fp_paged_attn(const fp_kv_cache *cache, const fp_batch *batch, int n_q_heads,

@@ -166,3 +166,30 @@ def test_workspaces_that_are_no_buffers_are_refused():
             serve.paged_attn(q, cache, b, ws=ws)
     with pytest.raises(ops.FPError, match="FP_ERR_WORKSPACE"):
         serve.paged_attn(q, cache, b, ws=torch.empty(n - 1, dtype=torch.uint8, device=DEV))
+
+
+# ------------------------------------------------- copies of 8-bit pages --
+
+@pytest.mark.parametrize("pages", [0, 3, 500])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 20)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chunks_over_8_bits_in_pools_of_any_size(pages, window, sinks, d):
+    """Bitwise the attention over a bf16 cache of the same values, in pools with
+    fewer and more pages than the table has places; two sequences share pages, one
+    page is missing, and the workspace held NaNs."""
+    kv_lens, q_lens, page, hq, hkv = [700, 333, 640], [70, 100, 130], 32, 8, 2
+    n_pages = sum(-(-x // page) for x in kv_lens) + pages
+    cache = make_cache(F8, n_pages, hkv, page, d, 4)
+    b, table, off = make_batch(kv_lens, q_lens, page, n_pages, 4)
+    b.page_table[2, :8] = b.page_table[0, :8]
+    b.page_table[1, 333 // page - 4] = n_pages
+    wide = serve.KVCache(*(torch.tensor(x, dtype=BF, device=DEV) for x in contents(cache)))
+    q = torch.randn(b.total_q * hq, d, generator=torch.Generator(device=DEV).manual_seed(2),
+                    device=DEV).to(BF)
+    ws = serve.workspace(cache, b, hq)
+    ws.fill_(255)
+    out, lse = serve.paged_attn(q, cache, b, window=window, sinks=sinks, ws=ws)
+    want, want_lse = serve.paged_attn(q, wide, b, window=window, sinks=sinks)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert out.isfinite().all()
+    assert serve.fp_serve_last_device_status() == DEVICE_CHECK

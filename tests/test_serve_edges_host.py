@@ -23,3 +23,16 @@ def test_fp32_queries_need_no_workspace(L):  # noqa: F811
     b = batch(max_q_len=100, total_q=200)
     assert paged(cache(**NARROW), b) == WS
     assert paged(cache(**NARROW), b, dtype=ops.FP_F32) in PAST
+
+
+def test_chunks_over_8_bits_copy_the_batchs_pages_not_the_pool(L):  # noqa: F811
+    def copies(**kw):
+        b = batch(max_q_len=100, total_q=200, **kw)
+        return (serve.fp_paged_attn_workspace(cache(n_pages=n_pages, **NARROW), b, 4)
+                - serve.fp_paged_attn_workspace(cache(n_pages=n_pages), b, 4))
+
+    page = 4 * 2 * 16 * 128  # of K and V, in bf16
+    n_pages = 2 ** 20
+    assert 0 <= copies() - 8 * page <= 1024  # (2 sequences of 4 pages; alignment)
+    n_pages = 5
+    assert 0 <= copies() - 5 * page <= 1024
