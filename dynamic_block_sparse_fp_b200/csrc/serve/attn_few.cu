@@ -315,14 +315,17 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
         factor[b][e] = scale2 * power(__shfl_sync(0xffffffffu, x, 4 * (2 * j4 + e)) - 28);
     }
   }
-  // pages of this unit that do not exist (their keys are hidden)
+  // pages of this unit that do not exist (their keys are hidden; that is an error
+  // where some row would see one)
   int missing = 0;
   for (int e = threadIdx.x; e < ntile * nbox; e += THREADS) {
-    const int key = kt.key(first_tile + e / nbox) + e % nbox * box;
-    if (key < seq.len && page_row(P, un.s, key >> P.shift, kv) < 0) missing = 1;
+    const int t0 = kt.key(first_tile + e / nbox), c = e % nbox * box, key = t0 + c;
+    if (key < seq.len && page_row(P, un.s, key >> P.shift, kv) < 0) {
+      missing = 1;
+      if (used_keys(P, seq, rt, t0) >> c & below(box)) report(status, FP_ERR_DEVICE_CHECK);
+    }
   }
   missing = __syncthreads_or(missing);
-  if (missing && threadIdx.x == 0) report(status, FP_ERR_DEVICE_CHECK);
   int pos[NB][2];
   float o[NB][HD / 16][4], m[NB][2], l[NB][2];
   // 8 bits: weights times their values' scales are 2^(t - mt), t a score plus the
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int e = 0; e < 2; ++e) seen[b][e] = seen_keys(P, pos[b][e], t0) & ~gone;
-      gone |= ~below(seq.len - t0);
+      gone |= ~used_keys(P, seq, rt, t0);
     }
     if (!__all_sync(0xffffffffu, bar_wait(&sm.full[slot], par, abort_flag))) {
       ok = false;
@@ -523,8 +526,8 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
                                        : pack_bf16(p[2 * n], p[2 * n + 1]));
       }
       // ------------------------------------------------------- V^T P^T --
-      // the halves of A's words whose keys nobody may read become 0 (whatever
-      // stands there, its weight of 0 would not hide a NaN)
+      // the halves of A's words whose keys no row sees become 0 (whatever stands
+      // there, a code of NaN too: its weight of 0 would not hide it)
       uint32_t keep0 = ~0u, keep1 = ~0u;
       if (part) {
         const uint32_t g16 = uint32_t(gone >> kb);

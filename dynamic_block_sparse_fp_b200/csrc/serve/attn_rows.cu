@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(threads_of(ROWS))
     }
     uint64_t hidden_pages = 0;
     if (!there) {
-      if (threadIdx.x == 0) report(status, FP_ERR_DEVICE_CHECK);
       hidden_pages = missing_keys(P, s, seq, t0);
+      if (threadIdx.x == 0 && (hidden_pages & used_keys(P, seq, rt, t0)))
+        report(status, FP_ERR_DEVICE_CHECK);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {

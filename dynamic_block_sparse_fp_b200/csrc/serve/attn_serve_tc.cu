@@ -226,15 +226,19 @@ __global__ void __launch_bounds__(THREADS, 2)
     *abort_flag = 1;
   };
   // The others wait for the barriers (2) and for each other's scan of the pages
-  // (3: who finds one of the unit's pages missing says so); the producer asks
-  // for the outcome (5) when the first loads are on their way.
+  // (3: who finds one of the unit's pages missing says so, an error where some row
+  // would see one of its keys); the producer asks for the outcome (5) when the first
+  // loads are on their way.
   auto begin = [&]() -> int {
     int missing = 0;
     const int id = warp < 4 ? threadIdx.x : threadIdx.x - 32;
     if (P.page != 0)
       for (int e = id; e < ntile * nbox; e += THREADS - 32) {
-        const int key = kt.key(first_tile + e / nbox) + e % nbox * box;
-        if (key < seq.len && page_row(P, un.s, key >> P.shift, kv) < 0) missing = 1;
+        const int t0 = kt.key(first_tile + e / nbox), c = e % nbox * box, key = t0 + c;
+        if (key < seq.len && page_row(P, un.s, key >> P.shift, kv) < 0) {
+          missing = 1;
+          if (used_keys(P, seq, rt, t0) >> c & below(box)) report(status, FP_ERR_DEVICE_CHECK);
+        }
       }
     named_barrier_sync(2, THREADS);
     if (missing) sm.missing = 1;
@@ -257,7 +261,6 @@ __global__ void __launch_bounds__(THREADS, 2)
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       const int missing = begin();
-      if (missing && threadIdx.x == 0) report(status, FP_ERR_DEVICE_CHECK);
       const uint32_t lane_base = sm.tmem_base + (uint32_t(warp * 32) << 16);
       {
         // the first 64 d of this row's query -> TMEM (A operand of Q K^T);

@@ -99,6 +99,14 @@ __device__ __forceinline__ uint64_t seen_keys(const Problem &P, int pos, int t0)
   return below(pos + 1 - t0) & (~below(low - t0) | below(P.sinks - t0));
 }
 
+// Bit c: some row of a tile sees key t0 + c (their windows' union: the positions are
+// consecutive).
+__device__ __forceinline__ uint64_t used_keys(const Problem &P, const Seq &q, const RowTile &rt,
+                                              int t0) {
+  const int p_lo = max(0, q.len - q.n + rt.t_lo), p_hi = q.len - q.n + rt.t_hi;
+  return below(p_hi + 1 - t0) & (~below(p_lo - P.window + 1 - t0) | below(P.sinks - t0));
+}
+
 // Bit c: key t0 + c lies in a page that does not exist.
 __device__ __forceinline__ uint64_t missing_keys(const Problem &P, int s, const Seq &q, int t0) {
   uint64_t m = 0;

@@ -44,7 +44,8 @@ enum { FP_E4M3 = 2 };
  *     ([n_pages, Hkv, page_size]): the vector's elements are
  *     code * 2^(byte - 127), byte 1 .. 254; byte 255 says that the whole vector
  *     is NaN.  The codes that stand for NaN, 0x7f and 0xff, and a byte of 0 must
- *     not occur in a sequence's vectors (fp_kv_write makes none).
+ *     not occur in vectors that a token sees or that are read (fp_kv_write makes
+ *     none).
  * k, v and the exps must be 16-byte aligned.
  */
 typedef struct {
@@ -78,7 +79,9 @@ typedef struct {
  * kv_lens[s] < 0 or > max_pages * page_size, is skipped (its rows of the
  * outputs are left as they were); a page outside 0 .. n_pages - 1 is not
  * read or written (its keys are not visible; fp_kv_read gives zeros for it).
- * Either records FP_ERR_DEVICE_CHECK.  Tokens at negative positions
+ * Either records FP_ERR_DEVICE_CHECK, in fp_paged_attn a page only if some of its
+ * keys would be seen: entries of pages that lie behind the window of every new
+ * token, and hold no sink, may be anything.  Tokens at negative positions
  * (n_s > kv_lens[s]) are not written by fp_kv_write, see nothing in
  * fp_paged_attn and read as zeros in fp_kv_read.  Rows at or past
  * q_offsets[n_seqs] are left as they were.

@@ -6,8 +6,8 @@ import math
 import numpy as np
 import pytest
 import torch
-from test_serve_gpu import (BF, DEV, F8, _lib, _status, check_group, contents,  # noqa: F401
-                            make_batch, make_cache, np64, sequence)
+from test_serve_gpu import (BF, DEV, F8, F32, _lib, _status, check_group,  # noqa: F401
+                            contents, make_batch, make_cache, np64, sequence)
 
 from dynamic_block_sparse_fp_b200 import ops, serve
 
@@ -192,4 +192,45 @@ def test_chunks_over_8_bits_in_pools_of_any_size(pages, window, sinks, d):
     want, want_lse = serve.paged_attn(q, wide, b, window=window, sinks=sinks)
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     assert out.isfinite().all()
+    assert serve.fp_serve_last_device_status() == DEVICE_CHECK
+
+
+# ------------------------------------------------ pages behind the window --
+
+@pytest.mark.parametrize("q_dtype,cache_dtype", [(BF, BF), (BF, F8), (F32, F32), (F32, F8)])
+@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("q_len,window,sinks", [(1, 90, 0), (1, 37, 20), (12, 90, 1), (12, 1, 0),
+                                                (70, 100, 0), (70, 25, 33)])
+def test_entries_behind_the_window_may_be_anything(q_dtype, cache_dtype, page, q_len, window,
+                                                   sinks):
+    """Pages that no new token sees were given back: their entries are no page
+    numbers, or another's page that holds bytes of all kinds.  That is no error, and
+    changes nothing."""
+    hq, hkv, d, kv_lens = 8, 2, 128, [1000, 300, 555]
+    n_pages = sum(-(-x // page) for x in kv_lens) + 1
+    cache = make_cache(cache_dtype, n_pages, hkv, page, d, 2)
+    b, table, off = make_batch(kv_lens, [q_len] * 3, page, n_pages, 2)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    q = torch.randn(b.total_q * hq, d, generator=g, device=DEV).to(q_dtype)
+    want, want_lse = serve.paged_attn(q, cache, b, window=window, sinks=sinks)
+    spare = (set(range(n_pages)) - {int(table[s, p]) for s in range(3)
+                                    for p in range(-(-kv_lens[s] // page))}).pop()
+    for x in (cache.k, cache.v):
+        x[spare] = math.nan  # (0x7f in 8 bits)
+    if cache_dtype == F8:
+        cache.k_exps[spare] = 0
+        cache.v_exps[spare] = 127
+    for entry in (-1, n_pages, spare):
+        for s, length in enumerate(kv_lens):
+            low = length - q_len - window + 1  # the first key of the first window
+            for p in range(-(-length // page)):
+                if (p + 1) * page <= low and p * page >= sinks:
+                    b.page_table[s, p] = entry
+        out, lse = serve.paged_attn(q, cache, b, window=window, sinks=sinks)
+        assert serve.fp_serve_last_device_status() == 0
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    # one page more is an error
+    low = kv_lens[0] - q_len - window + 1
+    b.page_table[0, low // page] = -1
+    serve.paged_attn(q, cache, b, window=window, sinks=sinks)
     assert serve.fp_serve_last_device_status() == DEVICE_CHECK
