@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
   // the slot's barrier expects all boxes.
   const int nb = 31 - __clz(nbox);
   auto box_row = [&](int t, int j) {
-    return tile_row(P, un.s, kv, seq.len, kt.key(first_tile + t) + j * box);
+    return tile_row<false>(P, un.s, kv, seq.len, kt.key(first_tile + t) + j * box);
   };
   auto expect = [&](int slot) {
     mbar_arrive_expect_tx(&sm.full[slot], 2 * G::TILE + (NARROW ? 2 * BN : 0));

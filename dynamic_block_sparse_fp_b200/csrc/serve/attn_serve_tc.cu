@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 2)
       auto fill = [&](int first) {
         const int c = first + lane;
         if (lane < 16 && c < total)
-          sm.rows[c % 64] = tile_row(P, un.s, kv, seq.len,
+          sm.rows[c % 64] = tile_row<true>(P, un.s, kv, seq.len,
                                      kt.key(first_tile + (c >> nb)) + (c & (nbox - 1)) * box);
       };
       if (lane == 0) {

@@ -59,13 +59,18 @@ __device__ __forceinline__ Seq load_seq(const Problem &P, int s) {
   return x;
 }
 
-// Row of (page, kv head, slot 0) of the keys and values, [pages * hkv * page, d], or
-// -1 for a page that does not exist.
+// Row of (page, kv head, slot 0) in the cache's [n_pages * hkv * page, d], or -1
+// for a page that does not exist.
 __device__ __forceinline__ long long page_row(const Problem &P, int s, int index, int kv) {
-  const long long place = static_cast<long long>(s) * P.max_pages + index;
-  const int id = P.table[place];
+  const int id = P.table[size_t(s) * P.max_pages + index];
   if (id < 0 || id >= P.n_pages) return -1;
-  return ((P.by_place ? place : id) * P.hkv + kv) * P.page;
+  return (static_cast<long long>(id) * P.hkv + kv) * P.page;
+}
+// The same where P.k and P.v may be copies by place.
+__device__ __forceinline__ long long held_row(const Problem &P, int s, int index, int kv) {
+  const long long row = page_row(P, s, index, kv);
+  if (!P.by_place || row < 0) return row;
+  return ((static_cast<long long>(s) * P.max_pages + index) * P.hkv + kv) * P.page;
 }
 
 // The 4 codes of a word times 2^(byte - 127), exact (NaN for byte 255).

@@ -291,10 +291,12 @@ __device__ __forceinline__ size_t first_part(const Split &sp, int kv) {
 
 // Row (of the K and V tensor maps) of the first of the keys key .. of one page,
 // or 0 where nothing may be read there: those keys are masked and zeroed.
+template <bool COPIES>  // P.k and P.v may be copies by place
 __device__ __forceinline__ int tile_row(const Problem &P, int s, int kv, int len, int key) {
   if (P.page == 0) return (s * P.hkv + kv) * len + key;
   if (key >= len) return 0;
-  const long long row = page_row(P, s, key >> P.shift, kv);
+  const long long row = COPIES ? held_row(P, s, key >> P.shift, kv)
+                               : page_row(P, s, key >> P.shift, kv);
   return row < 0 ? 0 : int(row) + (key & (P.page - 1));
 }
 
@@ -330,7 +332,7 @@ __device__ __forceinline__ void add_odd_values(const Problem &P, const Seq &seq,
   auto value_row = [&](int key) {
     const long long row = P.page == 0
                               ? (static_cast<long long>(s) * P.hkv + kv) * seq.len + key
-                              : page_row(P, s, key >> P.shift, kv) + (key & (P.page - 1));
+                              : held_row(P, s, key >> P.shift, kv) + (key & (P.page - 1));
     return reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(P.v) + row * HD);
   };
   auto is_odd = [](uint4 w) { return (odd16(w.x) | odd16(w.y) | odd16(w.z) | odd16(w.w)) != 0u; };
