@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
     prefetch_tmap(&tm_v);
   }
   // ------------------------------------------------------------- the unit --
-  const int crank = blockIdx.x % sp.cluster;  // of the CTAs that share a unit
+  const int crank = blockIdx.x % sp.cluster;  // of the CTAs that share an item
   Unit un = {int(blockIdx.z), int(blockIdx.x) / sp.cluster, 0, 1, 0, {}};
   if (sp.on) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -632,20 +632,13 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
   const bool whole = un.units == 1;
   const size_t part0 = whole ? 0 : (first_part(sp, kv) + un.part) * sp.rows;
   ok = ok && !*abort_flag;
-  // one row's result at 4 columns: out and lse, or the unit's partial result (whose
-  // maximum is -infinity where the row sees none of the unit's keys: any number in
-  // its place would be taken for a score when the units are joined)
+  // one row's result at 4 columns: out and lse
   auto store = [&](int r, int d, float big, float l, float4 x) {
-    if (whole) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      *reinterpret_cast<uint2 *>(out + (row0 + r) * HD + d) =
-          make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
-      if (lse && d == 0)
-        lse[row0 + r] = l == 0.f ? -INFINITY : (big + log2f(l)) * 0.6931471805599453f;
-    } else {
-      *reinterpret_cast<float4 *>(sp.part_o + (part0 + r) * HD + d) = x;
-      if (d == 0) sp.part_ml[part0 + r] = make_float2(big, l);
-    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *reinterpret_cast<uint2 *>(out + (row0 + r) * HD + d) =
+        make_uint2(pack_bf16(x.x * inv, x.y * inv), pack_bf16(x.z * inv, x.w * inv));
+    if (lse && d == 0)
+      lse[row0 + r] = l == 0.f ? -INFINITY : (big + log2f(l)) * 0.6931471805599453f;
   };
   for (int e = threadIdx.x; e < rt.rows * (HD / 4); e += THREADS) {
     const int r = e / (HD / 4), d = e % (HD / 4) * 4;
@@ -666,7 +659,13 @@ __global__ void __launch_bounds__(THREADS, Ring<HD, NARROW, RG>::CTAS)
       x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
     }
     if (!ok) l = 0.f, x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (sp.cluster == 1) {
+    if (!whole) {
+      // the unit's partial result, whose maximum is -infinity where the row sees none
+      // of its keys: any number in its place would be taken for a score when the
+      // units are joined
+      *reinterpret_cast<float4 *>(sp.part_o + (part0 + r) * HD + d) = x;
+      if (d == 0) sp.part_ml[part0 + r] = make_float2(big, l);
+    } else if (sp.cluster == 1) {
       store(r, d, big, l, x);
     } else {
       *reinterpret_cast<float4 *>(&sm.all_o[r][d]) = x;
@@ -798,11 +797,15 @@ Split few_split(const Problem &P, bool narrow) {
     if (items <= fit[i]) {
       // tiles for each CTA: 8 to 16, by how much of the machine the clusters use
       const int each = std::min(16, std::max(8, int(items) * sizes[i] / 10));
-      if (most_tiles(P) <= each * sizes[i])
-        return make_split<64>(P, each * sizes[i], 1, sizes[i], 2 * kSms);
+      if (most_tiles(P) <= each * sizes[i]) {
+        Split sp = {};
+        sp.cluster = sizes[i];
+        sp.tiles = most_row_tiles<64>(P);
+        return sp;
+      }
     }
   const int ctas = !narrow ? 2 : P.max_q_len * P.g > 8 ? 3 : 4;
-  return make_split<64>(P, 4, 4, 1, ctas * kSms);
+  return make_split<64>(P, 4, 4, ctas * kSms);
 }
 
 }  // namespace

@@ -676,7 +676,7 @@ cudaError_t run(const Problem &P, const Split &sp, const void *q, void *out, flo
 // with 2; 2 of 2000 tokens over 9000, 126: 392, 372).  Nor does it pay to have units
 // of less than 32 tiles.
 Split tc_split(const Problem &P) {
-  Split sp = make_split<BM>(P, LEAST, MIN_TILES, 1, 2 * kSms);
+  Split sp = make_split<BM>(P, LEAST, MIN_TILES, 2 * kSms);
   if (sp.pairs < 2 * sp.target) {
     const long long most = std::min(most_tiles(P), 1ll << 30) * sp.pairs / 32;
     sp.most = int(std::min(std::max<long long>(most, sp.target), 7ll * sp.target / 2));

@@ -21,7 +21,7 @@ struct Split {
   int min_tiles; // key tiles that a unit has at least
   int pairs, tiles;  // n_seqs * tiles, and row tiles per sequence
   int rows;      // rows of a partial result
-  int cluster;   // CTAs that share a unit
+  int cluster;   // CTAs that share an item (1 where units are found)
   int2 *plan;    // [pairs]: units, first partial
   float *part_o; // [partials][rows][d]
   float2 *part_ml;
@@ -83,8 +83,8 @@ __device__ __forceinline__ int pair_tiles(const Problem &P, const Split &sp, int
 // that their uneven ends overlap.  Or nothing is cut, where that should take less
 // time (stay_whole).
 //
-// find_unit finds the CTA's unit (blockIdx.x / cluster) of the kv head.  Every CTA computes
-// the same cut from the lengths.  Up to 32 items: every warp by itself, an item a
+// find_unit finds unit blockIdx.x of the kv head.  Every CTA computes the same cut
+// from the lengths.  Up to 32 items: every warp by itself, an item a
 // lane.
 __device__ __forceinline__ int first_size(const Split &sp, long long all, int units) {
   const unsigned most = unsigned(units);
@@ -155,12 +155,11 @@ __device__ __forceinline__ bool find_unit_warp(const Problem &P, const Split &sp
   // cut items' units come first, whole items (shorter) after them all
   const int cut = __shfl_sync(0xffffffffu, t, 31);
   u = units > 1 ? t : cut + u - t;
-  const int mine = blockIdx.x / sp.cluster;
+  const int mine = blockIdx.x;
   const unsigned owner = __ballot_sync(0xffffffffu, mine >= u - units && mine < u);
   if (owner == 0u) return false;
   const int who = __ffs(owner) - 1;
-  if (lane == who && threadIdx.x < 32 && mine == u - units && blockIdx.y == 0 &&
-      blockIdx.x % sp.cluster == 0)
+  if (lane == who && threadIdx.x < 32 && mine == u - units && blockIdx.y == 0)
     sp.plan[who] = make_int2(units, t - parts);
   const int k = mine - __shfl_sync(0xffffffffu, u - units, who);
   out->s = pair_seq(sp, who), out->x = who - out->s * sp.tiles, out->k = k;
@@ -253,7 +252,7 @@ __device__ __forceinline__ bool find_unit(const Problem &P, const Split &sp, Fin
   }
   // cut items' units come first, whole items (shorter) after them all
   u = cut + u - t;
-  const int mine = blockIdx.x / sp.cluster;
+  const int mine = blockIdx.x;
   if ((mine >= t && mine < t + parts) || (mine >= u && mine < u + units - parts)) {
     for (int p = p0; p < p1; ++p) {
       const int n = units_of(pair_tiles<ROWS>(P, sp, p), size);
@@ -261,8 +260,7 @@ __device__ __forceinline__ bool find_unit(const Problem &P, const Split &sp, Fin
       if (mine >= first && mine < first + n) {
         sm.unit[0] = pair_seq(sp, p), sm.unit[1] = p - sm.unit[0] * sp.tiles;
         sm.unit[2] = mine - first, sm.unit[3] = n, sm.unit[4] = t + (mine - first);
-        if (mine == first && blockIdx.y == 0 && blockIdx.x % sp.cluster == 0)
-          sp.plan[p] = make_int2(n, t);
+        if (mine == first && blockIdx.y == 0) sp.plan[p] = make_int2(n, t);
         break;
       }
       (n > 1 ? t : u) += n;
@@ -534,9 +532,9 @@ inline long long most_tiles(const Problem &P) {
 }
 
 template <int ROWS>
-Split make_split(const Problem &P, int least, int min_tiles, int cluster, int at_a_time) {
+Split make_split(const Problem &P, int least, int min_tiles, int at_a_time) {
   Split sp = {};
-  sp.cluster = cluster;
+  sp.cluster = 1;
   sp.tiles = most_row_tiles<ROWS>(P);
   const long long pairs = static_cast<long long>(P.n_seqs) * sp.tiles;
   if (P.page == 0 || pairs > kMaxPairs || most_tiles(P) <= least) return sp;
@@ -554,7 +552,7 @@ Split make_split(const Problem &P, int least, int min_tiles, int cluster, int at
 // more of them took 9 us of 117, a chunk of 700 tokens over 65536, window 4096.)
 inline dim3 grid_of(const Problem &P, const Split &sp) {
   if (!sp.on) return dim3(sp.tiles * sp.cluster, P.hkv, P.n_seqs);
-  return dim3((few_items(sp) ? sp.target : sp.pairs + sp.most) * sp.cluster, P.hkv, 1);
+  return dim3(few_items(sp) ? sp.target : sp.pairs + sp.most, P.hkv, 1);
 }
 
 inline size_t carve(const Problem &P, Split *sp, void *ws) {
