@@ -234,3 +234,133 @@ def test_entries_behind_the_window_may_be_anything(q_dtype, cache_dtype, page, q
     b.page_table[0, low // page] = -1
     serve.paged_attn(q, cache, b, window=window, sinks=sinks)
     assert serve.fp_serve_last_device_status() == DEVICE_CHECK
+
+
+# ------------------------------------------------------------ large batches --
+
+def check_some(out, lse, q, data, table, off, case, hq, hkv, which):
+    kv_lens, q_lens, page, window, sinks = case
+    d = q.shape[-1]
+    for s in which:
+        length, n = kv_lens[s], q_lens[s]
+        if n == 0:
+            continue
+        sl = slice(off[s] * hq, off[s + 1] * hq)
+        o, x = (np64(y[sl]).reshape(hkv, hq // hkv, n, d) for y in (out, q))
+        ls = np64(lse[sl]).reshape(hkv, hq // hkv, n)
+        k, v = (sequence(y, table, s, length, page) for y in data)
+        for h in range(hkv):
+            check_group(o[h], ls[h], x[h], k[h], v[h], length - n, window, sinks, BF)
+
+
+def run_all(cache, b, q, hq, window, sinks):
+    """paged_attn into outputs that were NaN: whatever is not written shows."""
+    out, lse = torch.full_like(q, math.nan), torch.full((len(q),), math.nan, device=DEV)
+    ws = serve.workspace(cache, b, hq)
+    assert serve.fp_paged_attn(cache.struct, b.struct, hq, ops.FP_BF16, window, sinks, q, out, lse,
+                               ws) == 0
+    assert not out.isnan().any() and not lse.isnan().any()
+    return out, lse
+
+
+@pytest.mark.parametrize("cache_dtype", [BF, F8])
+@pytest.mark.parametrize("hq,hkv,q_len", [(8, 2, 1), (16, 1, 3), (32, 2, 4)])
+@pytest.mark.parametrize("n_seqs,longest,slack", [(100, 200, 100), (100, 1500, 0), (1100, 100, 100),
+                                                  (1100, 40, 0)])
+def test_many_sequences_of_few_rows(cache_dtype, hq, hkv, q_len, n_seqs, longest, slack):
+    """Units and their join, and whole items, against the oracle; one sequence much
+    longer than the others."""
+    page = 16
+    kv_lens = [1 + (longest * (7 * s + 3)) // (7 * n_seqs) for s in range(n_seqs)]
+    kv_lens[n_seqs // 3] = 5000
+    q_lens = [max(0, q_len - s % 2) for s in range(n_seqs)]
+    case = (kv_lens, q_lens, page, 0, 0)
+    n_pages = sum(-(-x // page) for x in kv_lens) + 1
+    cache = make_cache(cache_dtype, n_pages, hkv, page, 128, n_seqs)
+    b, table, off = make_batch(kv_lens, q_lens, page, n_pages, n_seqs, slack_pages=slack)
+    g = torch.Generator(device=DEV).manual_seed(n_seqs)
+    q = torch.randn(b.total_q * hq, 128, generator=g, device=DEV).to(BF)
+    out, lse = run_all(cache, b, q, hq, 0, 0)
+    some = sorted({0, 2, 7, n_seqs // 3, n_seqs // 3 + 1, n_seqs // 2, n_seqs - 2, n_seqs - 1})
+    check_some(out, lse, q, contents(cache), table, off, case, hq, hkv, some)
+
+
+@pytest.mark.parametrize("cache_dtype", [BF, F8])
+@pytest.mark.parametrize("n_seqs,chunk,window", [(5, 1500, 0), (64, 2048, 0), (64, 2048, 333),
+                                                 (20, 700, 0)])
+def test_single_tokens_beside_a_chunk(cache_dtype, n_seqs, chunk, window):
+    """One sequence brings a chunk, the others a token each (one of them none)."""
+    hq, hkv, page = 8, 2, 64
+    kv_lens = [(37 * s * s) % 2900 + 1 for s in range(n_seqs)]
+    q_lens = [1] * n_seqs
+    kv_lens[2], q_lens[2], q_lens[1] = chunk + 500, chunk, 0
+    kv_lens[3] = 9000
+    case = (kv_lens, q_lens, page, window, 5)
+    n_pages = sum(-(-x // page) for x in kv_lens) + 1
+    cache = make_cache(cache_dtype, n_pages, hkv, page, 128, n_seqs)
+    b, table, off = make_batch(kv_lens, q_lens, page, n_pages, n_seqs)
+    g = torch.Generator(device=DEV).manual_seed(n_seqs)
+    q = torch.randn(b.total_q * hq, 128, generator=g, device=DEV).to(BF)
+    out, lse = run_all(cache, b, q, hq, window, 5)
+    check_some(out, lse, q, contents(cache), table, off, case, hq, hkv,
+               sorted({0, 2, 3, 4, n_seqs - 1}))
+
+
+def test_calls_repeat_themselves_bitwise():
+    """Every operator, twice on the same inputs with other calls between."""
+    for cache_dtype, q_len in ((BF, 1), (F8, 1), (BF, 150), (F8, 150)):
+        kv_lens, page = [9000, 200, 3333], 64
+        n_pages = sum(-(-x // page) for x in kv_lens)
+        cache = make_cache(cache_dtype, n_pages, 2, page, 128, 1)
+        b, _, _ = make_batch(kv_lens, [q_len] * 3, page, n_pages, 1)
+        g = torch.Generator(device=DEV).manual_seed(2)
+        q = torch.randn(b.total_q * 8, 128, generator=g, device=DEV).to(BF)
+        x = torch.randn(1, 4, 900, 128, generator=g, device=DEV).to(BF)
+        kv = torch.randn(b.total_q * 2, 128, generator=g, device=DEV).to(BF)
+        seen = []
+        for _ in range(3):
+            serve.kv_write(cache, b, kv, kv)
+            seen.append([*serve.paged_attn(q, cache, b), *serve.window_attn(x, x, x, 100, 4),
+                         *serve.kv_read(cache, b), cache.k.view(torch.uint8).clone()])
+        assert all(torch.equal(y, z) for later in seen[1:] for y, z in zip(seen[0], later))
+
+
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (8, 2), (32, 8), (24, 24)])
+@pytest.mark.parametrize("seed", range(6))
+def test_every_row_is_written_however_the_lengths_fall(hq, hkv, seed):
+    """The cut of random batches on the device: no row is left out (NaN), and each
+    sequence comes out as when it is called by itself, up to the weights' rounding
+    (2^-8 of the values' size each) and the output's, for both."""
+    rng = np.random.default_rng(seed)
+    page, d = 64, 64
+    n_pages = 700
+    cache = make_cache(BF, n_pages, hkv, page, d, seed)
+    top = float(cache.v.abs().max())
+    for _ in range(8):
+        n = int(rng.choice([1, 2, 5, 31, 32, 33, 70, 140, 500]))
+        longest = int(2 ** rng.uniform(2, 14))
+        kv_lens = [int(rng.choice([longest, rng.integers(0, longest + 1), 0])) for _ in range(n)]
+        most = int(rng.choice([1, 1, 3, 20, 300]))
+        q_lens = [int(rng.integers(0, most + 1)) for _ in range(n)]
+        q_lens[0] = most
+        # (pages are shared among the sequences)
+        table = rng.integers(0, n_pages, (n, longest // page + 1 + int(rng.choice([0, 50, 500]))))
+        table = torch.tensor(table, dtype=torch.int32, device=DEV)
+        off = np.concatenate([[0], np.cumsum(q_lens)])
+        b = serve.Batch(table, torch.tensor(kv_lens, dtype=torch.int32, device=DEV),
+                        torch.tensor(off, dtype=torch.int32, device=DEV), max_q_len=most,
+                        total_q=int(off[-1]))
+        q = torch.randn(b.total_q * hq, d, device=DEV).to(BF)
+        window = int(rng.choice([0, 0, 100]))
+        out, lse = run_all(cache, b, q, hq, window, 3)
+        for s in {0, n // 2, n - 1}:
+            if q_lens[s] == 0:
+                continue
+            one = serve.Batch(table[s:s + 1].contiguous(), b.kv_lens[s:s + 1].contiguous(),
+                              max_q_len=q_lens[s])
+            sl = slice(int(off[s]) * hq, int(off[s + 1]) * hq)
+            o, x = serve.paged_attn(q[sl].view(1, hq, q_lens[s], d), cache, one, window, 3)
+            assert (o.view(-1, d).float() - out[sl].float()).abs().max() <= 4 * 2.0 ** -8 * top
+            x, y = x.view(-1), lse[sl]
+            assert torch.equal(x.isinf(), y.isinf())
+            assert ((x - y)[~x.isinf()].abs() <= 1e-4 * (1 + y[~x.isinf()].abs())).all()

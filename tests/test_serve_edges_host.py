@@ -36,3 +36,13 @@ def test_chunks_over_8_bits_copy_the_batchs_pages_not_the_pool(L):  # noqa: F811
     assert 0 <= copies() - 8 * page <= 1024  # (2 sequences of 4 pages; alignment)
     n_pages = 5
     assert 0 <= copies() - 5 * page <= 1024
+
+
+def test_a_workspace_is_asked_for_and_its_size_checked(L):  # noqa: F811
+    b = batch(max_pages=4096)
+    for c in (cache(), cache(**NARROW)):
+        need = serve.fp_paged_attn_workspace(c, b, 4)
+        assert need > 0
+        assert paged(c, b) == WS
+        assert paged(c, b, ws=FAKE, ws_bytes=need - 1) == WS
+        assert paged(c, b, ws=FAKE + 128, ws_bytes=need) == WS
