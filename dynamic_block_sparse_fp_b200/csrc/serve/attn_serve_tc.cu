@@ -32,7 +32,7 @@
 //
 // 8-bit caches come here as bf16 copies of the pages that are read (kv_cache.cu):
 // converting tiles as they are loaded, by four more warps, took 390 us where
-// 171 us are enough (2048 new tokens, 32 heads over 2, window 4096), since every
+// 175 us are enough (2048 new tokens, 32 heads over 2, window 4096), since every
 // row tile converts its keys again.
 //
 // Every wait is bounded (2 s); on expiry the kernel records FP_ERR_TIMEOUT,

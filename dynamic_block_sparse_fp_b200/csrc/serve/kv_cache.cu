@@ -5,12 +5,13 @@
 // One vector (d elements of one token and head of K or V) is handled by a group of
 // neighbouring lanes, 8 elements each (of an 8-bit cache 16, which a read takes as 8
 // of each half, so that its stores are without gaps: 131072 tokens 143 us with 16 in
-// a row, 131 so).  The 8-bit scale of a vector needs its largest magnitude: an
+// a row, 132 so).  The 8-bit scale of a vector needs its largest magnitude: an
 // exchange among those lanes.  Every thread has AHEAD vectors in hand, whose page
 // numbers and elements are all asked for before the first is used.
 // Bound by DRAM: each element is read once and written once.  Measured (8 kv heads,
-// d 128): 32768 tokens into 8 bits 35 us (5.8 TB/s), 131072 out of 8 bits 131 us
-// (6.2 TB/s).
+// d 128): 32768 tokens into 8 bits 37 us (5.5 TB/s), 131072 out of 8 bits 132 us
+// (6.1 TB/s); 32768 of bf16 in 47 us, out 49 us (5.7 and 5.5 TB/s), of fp32 88 and 90
+// (6.1 and 6.0).
 #include "serve_internal.cuh"
 
 namespace fps {
@@ -96,8 +97,8 @@ __device__ __forceinline__ uint32_t exponent_byte(uint32_t amax) {
 }
 
 constexpr int AHEAD = 4;
-// (a vector on its way into 8 bits takes twice the registers; 32768 tokens: 35 us
-// with 2 a thread, 38 with 4, 45 with 8)
+// (a vector on its way into 8 bits takes twice the registers; 32768 tokens, against 2
+// a thread: 9 % longer with 4, 29 % with 8)
 template <class C>
 constexpr int write_ahead() {
   return sizeof(C) == 1 ? 2 : AHEAD;

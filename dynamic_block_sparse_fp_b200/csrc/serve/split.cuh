@@ -519,8 +519,11 @@ inline bool encode_map(CUtensorMap *map, const void *ptr, uint64_t rows, int d, 
 }
 
 // What the host knows of the cut (the lengths are on the device).  Nothing is cut
-// where no item can have more than `least` tiles, nor beyond kMaxPairs row tiles: the
-// machine is full then, and the search for a unit would cost more than the cut gains.
+// where no item can have more than `least` tiles, nor beyond kMaxPairs row tiles, where
+// every CTA's search for its unit would cost more than the cut gains: so many items
+// fill the machine, unless most of them are short or empty (max_q_len is the longest
+// sequence's: one long chunk among single tokens counts as many).  Then a long item is
+// walked by one CTA, at some 1500 cycles for each 64 keys of a chunk's kernel.
 constexpr int kMaxPairs = 1024, kSms = 148;
 
 // Longest list of key tiles that an item can have.

@@ -18,8 +18,10 @@
  *     window <= 0,  or  i - j < window,  or  j < sinks.
  * Attention is softmax(q.k / sqrt(d)) over the visible keys, in fp32 (bf16
  * inputs: tensor-core products with fp32 accumulation, the softmax weights
- * rounded to bf16 for the product with V; fp32 inputs: fp32 throughout, the
- * debug path).  What is not visible has no influence, a NaN or an infinity
+ * rounded to bf16 for the product with V, or, for few rows over an 8-bit cache
+ * (max_q_len * Hq / Hkv <= 64), weights times the values' scales rounded to fp16 and
+ * queries held in fp16 with a power of two for each row; fp32 inputs: fp32
+ * throughout, the debug path).  What is not visible has no influence, a NaN or an infinity
  * there included.  A query that sees nothing gets zeros and lse = -inf.  `lse`
  * (or NULL) is the natural-log sum of exponentials of the scaled logits, fp32.
  */
@@ -123,7 +125,8 @@ fp_status fp_kv_write(const fp_kv_cache *cache, const fp_batch *batch, fp_dtype 
 /*
  * fp_kv_read -- the inverse: the newest n_s tokens of every sequence, packed,
  * of type dtype (the cache's own; FP_BF16 or FP_F32 from FP_E4M3, exact but for
- * bf16 values below 2^-126).  With n_s = kv_lens[s]: whole sequences, laid out
+ * bf16 values below 2^-126, and for 2^128, as which values above 248 * 2^120 are
+ * held and which reads as an infinity).  With n_s = kv_lens[s]: whole sequences, laid out
  * for the calls of fp.h.
  */
 fp_status fp_kv_read(const fp_kv_cache *cache, const fp_batch *batch, fp_dtype dtype, void *k,
